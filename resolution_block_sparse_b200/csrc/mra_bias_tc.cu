@@ -15,8 +15,11 @@
 // row: one takes a step's first, the other its second block.  A thread reads
 // its row's 32 scores and writes the weights back over them in bf16, the A
 // operand of the second product.  A pair of row and block outside the lists
-// costs no exponential.  The two warps of a row share nothing in the loop:
-// forward, each has a reference, a sum and an output accumulator of its own,
+// costs no exponential, and the products leave out its 32 rows (by the lanes
+// that they may write): with weights of 0 in their place, a NaN or an infinity
+// in V, K, Q or dO would reach rows whose lists do not hold it.  So the
+// accumulators are zeros at an item's start, which its last reader sees to.
+// The two warps of a row share nothing in the loop: forward, each has a reference, a sum and an output accumulator of its own,
 // joined at the end.
 //
 // Forward and delta have two buffers of scores in tensor memory: the next
@@ -61,7 +64,7 @@ namespace {
 
 using tc::mma_commit;
 using tc::mma_f16;
-using tc::mma_f16_ts;
+using tc::mma_f16_ts_rows;
 using tc::sdesc;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
@@ -102,6 +105,7 @@ struct ItemInfo {
     BlockInfo info;
     int bucket[kMode == kRows ? kTcRows : 1][kMaxChunk];
     float stat[kMode == kRows ? 2 : 1][kMode == kDelta || kMode == kRows ? kTileRows : 1];   // minus lse, minus delta
+    uint32_t rows_off[kTcRows];   // kRows, kCols: the item's rows without a gradient (padded)
 };
 
 template <int kMode>
@@ -353,6 +357,10 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                     }
                 }
             }
+            if ((kMode == kRows || cols) && it.bh >= 0 && lane < kTcRows) {
+                const int row = it.group * kTcRows + lane;
+                x.rows_off[lane] = row < c.nbr ? ~c.valid[it.bh / c.H * c.nbr + row] : 0xffffffffu;
+            }
             if (lane == 0) x.it = it;
             __syncwarp();
             if (lane == 0) mbar_arrive(saddr(&s.item_full[n & 1]));
@@ -397,7 +405,20 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
         const uint64_t a1 = sdesc(saddr(s.a[0]), 16, 1024), a2 = sdesc(saddr(s.a[S::two ? 1 : 0]), 16, 1024);
         const uint64_t b1 = sdesc(saddr(s.b[0][0]), 16, 1024), b2 = sdesc(saddr(s.b[0][1]), 16, 1024);
         constexpr uint64_t kStage = (uint64_t)(2 * S::stack * kTileBytes) >> 4;
-        // products of step t's weights; first: the item's first step
+        // the rows that do not list each of a step's k blocks (found before the
+        // step's weights are awaited)
+        uint32_t off_rows[S::stack][kTcRows];
+        auto rows_of = [&](const ItemInfo<kMode> &x, int st, int k) {
+#pragma unroll
+            for (int j = 0; j < S::stack; ++j) {
+                const int e = j < k ? x.info.entry[st * S::stack + j] : 0;
+#pragma unroll
+                for (int r = 0; r < kTcRows; ++r)
+                    off_rows[j][r] = (kMode == kForward ? 0u : x.rows_off[r]) | (((e >> (kMemberShift + r)) & 1) ? 0u : 0xffffffffu);
+            }
+        };
+        // products of step t's weights; first: the item's first step (its
+        // accumulators are zeros)
         auto accumulate = [&](int t, int k, bool first, int item) -> bool {
             const int sg = t % kStages, buf = t % kBuffers;
             if (!wait_warp(&s.weights[buf], (t / kBuffers) & 1)) return false;
@@ -420,10 +441,9 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                     const uint64_t off = (uint64_t)(j * kTileBytes + kk * 2048) >> 4;
                     // forward: each half of a row's blocks has its own accumulator
                     const uint32_t acc = kColAcc + (kMode == kForward ? 64 * j : 0);
-                    const uint32_t more = (kMode != kForward && j > 0) || kk > 0 ? 1u : first ? 0u : 1u;
                     const uint32_t from = w + 32 * j + (cols ? 16 : 8) * kk;     // kCols: P, then dS, 16 columns each
-                    mma_f16_ts(tmem + acc, from + (cols ? 8 : 0), src1 + off, kIdescAcc, more);
-                    if (cols) mma_f16_ts(tmem + kColAcc + 64, from, src2 + off, kIdescAcc, more);
+                    mma_f16_ts_rows(tmem + acc, from + (cols ? 8 : 0), src1 + off, kIdescAcc, off_rows[j]);
+                    if (cols) mma_f16_ts_rows(tmem + kColAcc + 64, from, src2 + off, kIdescAcc, off_rows[j]);
                 }
                 mma_commit(saddr(&s.empty[sg]));
             }
@@ -437,10 +457,16 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
             // (a reduction's result is known to be the same in every lane)
             const int count = __reduce_max_sync(0xffffffffu, s.item[n & 1].it.bh < 0 ? -1 : s.item[n & 1].it.count);
             const int steps = steps_of(max(count, 0));
-            __syncwarp();
-            if (elect_one()) mbar_arrive(saddr(&s.item_empty[n & 1]));
+            const ItemInfo<kMode> &x_item = s.item[n & 1];
+            auto item_done = [&]() {
+                __syncwarp();
+                if (elect_one()) mbar_arrive(saddr(&s.item_empty[n & 1]));
+            };
             if (count < 0) break;
-            if (steps == 0) continue;
+            if (steps == 0) {
+                item_done();
+                continue;
+            }
             if (!(ok = wait_warp(&s.a_full, na & 1))) break;
             // A1 (or A2) times a step's B1 (B2): 32 columns for each of its blocks
             auto product = [&](int st, int tt, uint32_t to, uint64_t a, uint64_t b) {
@@ -476,6 +502,7 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                 for (int st = 0; st + 1 < steps; ++st, ++t) {
                     if (!(ok = wait_warp(&s.full[(t + 1) % kStages], ((t + 1) / kStages) & 1))) break;
                     if (kMode == kRows) scores_x(st + 1, t + 1);
+                    rows_of(x_item, st, S::stack);
                     if (!(ok = wait_warp(&s.weights[t % kBuffers], (t / kBuffers) & 1))) break;
                     tc_fence_after();
                     if (kMode == kRows) scores_dp(st + 1, t + 1);
@@ -501,13 +528,19 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                         if (st == steps - 1) mma_commit(saddr(&s.a_empty));
                     }
                     __syncwarp();
-                    if (st > 0 && !(ok = accumulate(t - 1, S::stack, st == 1, na))) break;
+                    if (st > 0) {
+                        if (kMode != kDelta) rows_of(x_item, st - 1, S::stack);
+                        if (!(ok = accumulate(t - 1, S::stack, st == 1, na))) break;
+                    }
                 }
             }
             if (!ok) break;
             // the last step's at once: the item's end waits for it, and the
             // next item's first scores for its tiles
-            ok = accumulate(t - 1, count - (steps - 1) * S::stack, steps == 1, na);
+            const int last = count - (steps - 1) * S::stack;
+            if (kMode != kDelta) rows_of(x_item, steps - 1, last);
+            ok = accumulate(t - 1, last, steps == 1, na);
+            item_done();
             ++na;
         }
         // every product issued here completes before tensor memory is freed
@@ -523,6 +556,19 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
         const int row = quarter * 32 + lane, nb = c.buckets;
         float *const my_bins = bins + (kMode == kRows ? warp * nb : 0);
         float *const my_diag = s.diag[kMode == kRows ? warp : 0];
+        // this warp's part of the accumulators, zeros at every item's start
+        auto clear = [&]() {
+            const uint32_t zero[8] = {};
+            const uint32_t own = lanes + kColAcc + (cols ? 64 : 32) * half;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                tmem_st8(own + 8 * k, zero);
+                if (kMode == kForward) tmem_st8(own + 64 + 8 * k, zero);
+                if (cols) tmem_st8(own + 32 + 8 * k, zero);
+            }
+            tmem_wait_st();
+        };
+        if (kMode != kDelta) clear();
         int t = 0;
         for (int n = 0;; ++n) {
             const ItemInfo<kMode> &x_item = s.item[n & 1];
@@ -573,13 +619,6 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                 if (!((entry >> (kMemberShift + quarter)) & 1)) {
                     if (S::split && !(ok = wait_warp(&s.scores_dp, t & 1))) break;
                     tc_fence_after();
-                    if (kMode != kDelta && i < it.count) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = 0u;
-                        tmem_st16(cols ? at_dp : at, w);
-                        if (cols) tmem_st16(at_dp + 16, w);
-                    }
                 } else {
                     const int other = (entry & 0xffff) * kTokens;
                     const float u = x_item.info.tile[quarter][i];
@@ -755,6 +794,7 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
             }
             if (kMode != kDelta && steps > 0) {
                 // the accumulators are free for the next item
+                clear();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(saddr(&s.acc_empty));
