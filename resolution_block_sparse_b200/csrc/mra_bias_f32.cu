@@ -98,33 +98,44 @@ __device__ __forceinline__ void mul_abt(float (&x)[4][4], const float *a, const 
 }
 
 // acc[i][.] += weights of row ty + 16 i (shared, 32 of them) times the rows of
-// b; a thread's columns are 4 tx + 32 k .. + 3
-template <int D>
-__device__ __forceinline__ void mul_ab(float (&acc)[4][D / 8], const float *w, const float *b, int ty, int tx) {
+// b, for kRows rows i from kFirst on; a thread's columns are 4 tx + 32 k .. + 3
+template <int D, int kFirst, int kRows>
+__device__ __forceinline__ void mul_ab_of(float (&acc)[4][D / 8], const float *w, const float *b, int ty, int tx) {
     constexpr int kPitch = D + 4;
 #pragma unroll 2
     for (int n = 0; n < kTokens; n += 4) {
-        float4 p[4];
+        float4 p[kRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(w + (ty + 16 * i) * kPitchS + n);
+        for (int i = 0; i < kRows; ++i) p[i] = *reinterpret_cast<const float4 *>(w + (ty + 16 * (kFirst + i)) * kPitchS + n);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 const float4 v = *reinterpret_cast<const float4 *>(b + (n + m) * kPitch + 32 * k + 4 * tx);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kRows; ++i) {
+                    float *const a = acc[kFirst + i] + 4 * k;
                     const float f = m == 0 ? p[i].x : m == 1 ? p[i].y : m == 2 ? p[i].z : p[i].w;
-                    const float2 lo = fma2(both(f), make_float2(v.x, v.y), make_float2(acc[i][4 * k], acc[i][4 * k + 1]));
-                    const float2 hi = fma2(both(f), make_float2(v.z, v.w), make_float2(acc[i][4 * k + 2], acc[i][4 * k + 3]));
-                    acc[i][4 * k] = lo.x;
-                    acc[i][4 * k + 1] = lo.y;
-                    acc[i][4 * k + 2] = hi.x;
-                    acc[i][4 * k + 3] = hi.y;
+                    const float2 lo = fma2(both(f), make_float2(v.x, v.y), make_float2(a[0], a[1]));
+                    const float2 hi = fma2(both(f), make_float2(v.z, v.w), make_float2(a[2], a[3]));
+                    a[0] = lo.x;
+                    a[1] = lo.y;
+                    a[2] = hi.x;
+                    a[3] = hi.y;
                 }
             }
         }
     }
+}
+
+// The same for the block rows (members) that list the block, rows i = 0, 1 and
+// 2, 3: another row's weights are 0, and 0 times a NaN of a block that it does
+// not list must not be formed.
+template <int D>
+__device__ __forceinline__ void mul_ab(float (&acc)[4][D / 8], const float *w, const float *b, int ty, int tx, int members) {
+    if (members == 3) mul_ab_of<D, 0, 4>(acc, w, b, ty, tx);
+    else if (members == 1) mul_ab_of<D, 0, 2>(acc, w, b, ty, tx);
+    else mul_ab_of<D, 2, 2>(acc, w, b, ty, tx);
 }
 
 __device__ __forceinline__ void put_weights(float *w, const float (&x)[4][4], int ty, int tx) {
@@ -267,7 +278,10 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
             u[k] = next_u[k];
             tb[k] = next_tb[k];
         }
-        const int cpos = (entry & 0xffff) * kTokens;
+        const int cpos = (entry & 0xffff) * kTokens, members = entry >> kMemberShift;
+        bool row_on[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row_on[i] = ((members >> (i >> 1)) & 1) && ((on[i >> 1] >> ((ty + 16 * i) & 31)) & 1u);
         if (n + 1 < it.count) {
             next_entry = list[it.start + n + 1];
             fetch(buf ^ 1);
@@ -281,11 +295,10 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty + 16 * i;
-            const bool row_on = ((entry >> (kMemberShift + (i >> 1))) & 1) && ((on[i >> 1] >> (r & 31)) & 1u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int d = cpos + tx + 8 * j - pos - r;
-                const bool ok = row_on && ((cv >> (tx + 8 * j)) & 1u);
+                const bool ok = row_on[i] && ((cv >> (tx + 8 * j)) & 1u);
                 const float bias = u[i >> 1] == INFINITY ? __ldg(vec + (cols ? -d : d)) : u[i >> 1];
                 x[i][j] = ok ? fmaf(x[i][j], c.scale, bias) : -INFINITY;
             }
@@ -309,7 +322,7 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
                 }
             }
             put_weights(s.x, x, ty, tx);
-            mul_ab<D>(acc, s.x, s.b2[buf], ty, tx);
+            mul_ab<D>(acc, s.x, s.b2[buf], ty, tx, members);
             __syncthreads();
             continue;
         }
@@ -319,10 +332,11 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = fast_exp2((x[i][j] + (cols ? s.stat[buf][0][tx + 8 * j] : nlse[i])) * kLog2e);
-                if (kMode == kDelta) l[i] = fmaf(p, dp[i][j], l[i]);
+                // (a row that takes no part has weight 0, and its dP may be a NaN)
+                const float p = row_on[i] ? fast_exp2((x[i][j] + (cols ? s.stat[buf][0][tx + 8 * j] : nlse[i])) * kLog2e) : 0.0f;
+                if (kMode == kDelta && row_on[i]) l[i] = fmaf(p, dp[i][j], l[i]);
                 x[i][j] = p;
-                dp[i][j] = p * (dp[i][j] + (cols ? s.stat[buf][1][tx + 8 * j] : ndelta[i]));
+                dp[i][j] = row_on[i] ? p * (dp[i][j] + (cols ? s.stat[buf][1][tx + 8 * j] : ndelta[i])) : 0.0f;
             }
         if (kMode == kDelta) {
             __syncthreads();
@@ -330,10 +344,10 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
         }
         if constexpr (kMode == kCols) {
             put_weights(s.x, x, ty, tx);
-            mul_ab<D>(acc2, s.x, s.b2[buf], ty, tx);
+            mul_ab<D>(acc2, s.x, s.b2[buf], ty, tx, members);
         }
         put_weights(s.x, dp, ty, tx);
-        mul_ab<D>(acc, s.x, s.b1[buf], ty, tx);
+        mul_ab<D>(acc, s.x, s.b1[buf], ty, tx, members);
         if (kMode == kRows) {
             bool several = false;
 #pragma unroll
@@ -471,8 +485,13 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f[i] = c.scale;
+        const int r = ty + 16 * i, n = pos + r;
+        if (kMode != kFwd && !((on[i >> 1] >> (r & 31)) & 1u)) {
+            // a padded row has no gradient, whatever its blocks hold
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) acc[i][k] = acc2[kMode == kCols ? i : 0][k] = 0.0f;
+        }
         if (kMode == kFwd) {
-            const int r = ty + 16 * i, n = pos + r;
             const bool live = ((on[i >> 1] >> (r & 31)) & 1u) && l[i] > 0.0f;
             f[i] = live ? 1.0f / l[i] : 0.0f;
             if (!live)

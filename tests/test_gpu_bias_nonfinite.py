@@ -25,7 +25,11 @@ BF16, F32 = torch.bfloat16, torch.float32
 TC = {"tc-lists": dict(B=8, H=8, N=1100, D=64, dtype=BF16, lists=rows(9, (1, 2), (0, 5)), pad=[0, 300] + [0] * 6),
       "tc-long-rows": dict(B=20, H=8, N=700, D=64, dtype=BF16, lists=rows(9, (), (0, 9))),
       "tc-causal": dict(B=20, H=16, N=161, D=64, dtype=BF16, causal=True)}
-CASES = {**TC}
+FP32 = {"f32-lists": dict(B=2, H=3, N=700, D=64, dtype=F32, lists=rows(6, (1, 2), (0, 5)), pad=[0, 200]),
+        "f32-lists-d32": dict(B=2, H=2, N=500, D=32, dtype=F32, lists=rows(3, (1, 2), (0, 9)), pad=[100, 0]),
+        "f32-causal": dict(B=2, H=2, N=161, D=64, dtype=F32, causal=True),
+        "f32-causal-d32": dict(B=1, H=4, N=300, D=32, dtype=F32, causal=True)}
+CASES = {**TC, **FP32}
 
 
 def make(name, seed=5):
@@ -89,7 +93,7 @@ def test_reach(name, where, value):
     # and what it does reach is not hidden
     if where == "v":
         pairs = (with_pair(p, token) & live).nonzero(as_tuple=True)
-        assert not bool(torch.isfinite(got["out"][pairs][:, 5].float()).any())
+        assert not bool(torch.isfinite(got["out"][pairs][:, 5]).any())
     if where == "dout" and value != value:
         i = on.reshape(B, H, nbr, nbr)[:, :, J]
         dv = got["dv"][..., 5].float().isnan()
