@@ -255,6 +255,10 @@ MRA_API int mra_bigbird_block_list(int N, int block_size, int num_random, const 
  *     fp32 by dtype; D is 32 or 64.  fp32 runs without TF32.
  *   key_mask: as above; padded tokens are masked as keys and as queries.
  *     What padded rows of q, k, v and dout hold does not matter.
+ *   A NaN or an infinity in a valid token reaches the queries (the keys) of
+ *     the block rows (columns) whose listed blocks join them to its block, and
+ *     no others; there it also reaches pairs that the table or the bucket map
+ *     excludes, but no padded token.
  *   bias_table: DEVICE [num_buckets][H] in the element type of q, 1 <=
  *     num_buckets <= 1024.  A value at or below -1e30 (-inf among them)
  *     excludes its pairs: they get no weight and pass no gradient.

@@ -93,6 +93,18 @@ __device__ __forceinline__ float2 residual(float2 v) {
     return make_float2(v.x - __uint_as_float(h << 16), v.y - __uint_as_float(h & 0xffff0000u));
 }
 
+// Zeros the fragment rows of a warp's 16 x D result that are padded: they have no
+// gradient, whatever the blocks that they meet hold (0 times a NaN among it).
+template <int D>
+__device__ __forceinline__ void clear_padded(float (&acc)[D / 8][4], uint32_t rows_on, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if ((rows_on >> ((lane >> 2) + 8 * i)) & 1u) continue;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) acc[t][2 * i] = acc[t][2 * i + 1] = 0.0f;
+    }
+}
+
 template <int D, bool kDelta>
 __global__ void __launch_bounds__(kWarpThreads, 3)
 row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
@@ -316,6 +328,7 @@ row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
                 }
             }
         }
+        clear_padded<D>(acc[0], rows_on, lane);
         if (ok && write)
             store_rows<D>(s.q[0], wrow, acc[0], c.scale, c.scale, dq + ((size_t)it.bh * c.N + qpos) * D, c.N - qpos, lane);
     }
@@ -485,6 +498,8 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
     }
     if (ok) {
         const size_t at = ((size_t)it.bh * c.N + kpos) * D;
+        clear_padded<D>(ak[0], keys_on, lane);
+        clear_padded<D>(av[0], keys_on, lane);
         store_rows<D>(s.kv[0], wrow, ak[0], c.scale, c.scale, dk + at, c.N - kpos, lane);
         store_rows<D>(s.kv[1], wrow, av[0], 1.0f, 1.0f, dv + at, c.N - kpos, lane);
     }

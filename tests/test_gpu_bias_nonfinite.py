@@ -29,7 +29,14 @@ FP32 = {"f32-lists": dict(B=2, H=3, N=700, D=64, dtype=F32, lists=rows(6, (1, 2)
         "f32-lists-d32": dict(B=2, H=2, N=500, D=32, dtype=F32, lists=rows(3, (1, 2), (0, 9)), pad=[100, 0]),
         "f32-causal": dict(B=2, H=2, N=161, D=64, dtype=F32, causal=True),
         "f32-causal-d32": dict(B=1, H=4, N=300, D=32, dtype=F32, causal=True)}
-CASES = {**TC, **FP32}
+WARP = {"warp-lists-d32": dict(B=2, H=4, N=700, D=32, dtype=BF16, lists=rows(6, (1, 2), (0, 5)), pad=[0, 300]),
+        "warp-half-listed-d32": dict(B=1, H=2, N=500, D=32, dtype=BF16, lists=rows(11, (1, 2), (0, 9)), pad=[100]),
+        "warp-causal-d32": dict(B=2, H=2, N=161, D=32, dtype=BF16, causal=True),
+        "warp-long-causal-d32": dict(B=1, H=1, N=1200, D=32, dtype=BF16, causal=True),
+        "warp-padded-d32": dict(B=3, H=2, N=150, D=32, dtype=BF16, pad=[70, 0, 33]),
+        "warp-backward": dict(B=2, H=2, N=400, D=64, dtype=BF16, lists=rows(3, (1,), (0, 5)), pad=[0, 150]),
+        "warp-backward-causal": dict(B=1, H=2, N=300, D=64, dtype=BF16, causal=True, pad=[90])}
+CASES = {**TC, **FP32, **WARP}
 
 
 def make(name, seed=5):
