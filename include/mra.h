@@ -274,7 +274,8 @@ MRA_API int mra_bigbird_block_list(int N, int block_size, int num_random, const 
  *     ascending or out of range sets MRA_DEV_COUNT, gets no output (out, lse,
  *     dq, dk, dv are not written for it) and adds nothing to dbias_table.
  *   Queries without a pair (padded, empty rows, all excluded): out 0, lse
- *     -inf, no gradient.
+ *     -inf, no gradient.  A query with a NaN or +inf among its scores: out, lse
+ *     and its gradient NaN.
  *   workspace: DEVICE, 256-byte aligned, at least as many bytes as
  *     mra_blocksparse_attention_bias_workspace says for the same sizes
  *     (cap_sel 0: block_idx NULL; backward 0 or 1); MRA_ERR_TOO_LARGE when it

@@ -492,7 +492,7 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
             for (int k = 0; k < D / 8; ++k) acc[i][k] = acc2[kMode == kCols ? i : 0][k] = 0.0f;
         }
         if (kMode == kFwd) {
-            const bool live = ((on[i >> 1] >> (r & 31)) & 1u) && l[i] > 0.0f;
+            const bool live = ((on[i >> 1] >> (r & 31)) & 1u) && l[i] != 0.0f;      // (NaN: live)
             f[i] = live ? 1.0f / l[i] : 0.0f;
             if (!live)
 #pragma unroll

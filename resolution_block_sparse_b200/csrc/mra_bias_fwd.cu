@@ -252,7 +252,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int n = 16 * i + 8 * k + g;
-                const bool live = ((rows_on >> n) & 1u) && sum[i][k] > 0.0f;
+                const bool live = ((rows_on >> n) & 1u) && sum[i][k] != 0.0f;      // (NaN: live)
                 f[k] = live ? 1.0f / sum[i][k] : 0.0f;
                 if (!live) {
 #pragma unroll

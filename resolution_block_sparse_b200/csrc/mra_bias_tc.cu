@@ -880,7 +880,7 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                 } else if (pos < c.N) {
                     float f = cols && half == 1 ? 1.0f : c.scale;
                     if (kMode == kForward) {
-                        const bool live = row_on && total > 0.0f;
+                        const bool live = row_on && total != 0.0f;      // (NaN: live)
                         f = 1.0f / total;
                         if (!live) {
                             f = 0.0f;

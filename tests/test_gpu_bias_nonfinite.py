@@ -113,3 +113,34 @@ def with_pair(p, token):
     on = tokens(listed(p)[:, :, token // 32], N).reshape(B, H, N)
     d = token - torch.arange(N, device="cuda") + N - 1
     return on & (p.bucket[d] >= 0)[None, None]
+
+
+@pytest.mark.parametrize("name", list(CASES))
+@pytest.mark.parametrize("where", ["q", "k", "table"])
+def test_rows_with_a_nan_score_are_nan(name, where):
+    """A query whose scores hold a NaN has pairs: its output and lse are NaN, not
+    the 0 and -inf of a query without one, and so is its gradient."""
+    p = make(name)
+    B, H, N, D = p.q.shape
+    token = N // 2 + 3
+    live = torch.ones(B, N, dtype=torch.bool, device="cuda") if p.mask is None else p.mask > 0
+    live = live[:, None].expand(B, H, N)
+    any_pair = p.want()["lse"][0] > -math.inf
+    if where == "q":
+        hit = torch.zeros(B, H, N, dtype=torch.bool, device="cuda")
+        hit[:, :, token] = True
+    elif where == "k":
+        hit = with_pair(p, token)
+    else:
+        # bucket 0: the query's own position
+        on = listed(p).diagonal(dim1=1, dim2=2)
+        hit = tokens(on, N).reshape(B, H, N)
+    hit = hit & live & any_pair
+    if where == "table":
+        p.table[0] = math.nan
+    else:
+        getattr(p, where)[:, :, token, 3] = math.nan
+    got = p.both()
+    assert bool(hit.any())
+    assert bool(got["out"][hit].isnan().all()) and bool(got["lse"][hit].isnan().all())
+    assert bool(got["dq"][hit].isnan().all())
