@@ -27,8 +27,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace mra {
 namespace bias {
 
@@ -201,20 +199,6 @@ __device__ __forceinline__ void table_gradient(const Call &c, int warps) {
 inline size_t forward_part_floats(int D, int group) { return 32 * (size_t)group * (D + 16); }
 inline size_t row_part_floats(int D, int group, int buckets) { return 32 * (size_t)group * D + (size_t)buckets; }
 inline size_t col_part_floats(int D, int group) { return 64 * (size_t)group * D; }
-
-// Lets `kernel` have up to `bytes` of shared memory (the most that any call
-// asks for); once per device, as `done` records.
-template <typename K>
-cudaError_t allow_shared(K *kernel, size_t bytes, std::atomic<unsigned long long> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
 
 cudaError_t launch_prepare(const Call &c, bool bf16, bool columns, cudaStream_t s, int *launches);
 // bf16 over every block of at most kDirectBlocks blocks: one launch that makes

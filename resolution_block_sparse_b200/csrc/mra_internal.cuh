@@ -16,6 +16,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <utility>
 
 #include <cuda_runtime.h>
@@ -136,6 +137,20 @@ struct Workspace {
 
 // Number of SMs of the current device (cached per device; thread-safe).
 int device_sm_count();
+
+// Lets `kernel` have up to `bytes` of shared memory (the most that any call
+// asks for); once per device, as `done` records.
+template <typename K>
+cudaError_t allow_shared(K *kernel, size_t bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // For entry points outside mra_api.cu: the status word of the current device
 // (allocated on first use; an mra_status value) and the launch count that

@@ -355,8 +355,12 @@ cudaError_t forward(const Args &a, cudaStream_t s) {
     constexpr int kThreads = kTpr == 32 ? 128 : kTpr;
     auto *kern = norm_forward_kernel<T, V, kPer, kTpr, kThreads>;
     const int smem = 4 * weight_stride(a.hidden, V, kTpr == 32) * (int)sizeof(typename Weight<T, kTpr == 32>::type);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the limit of the longest row that this instance takes, not of this call's:
+    // another thread may launch it between the two
+    constexpr int kMost = 4 * weight_stride(std::min(kMaxHidden, kPer * kTpr * V), V, kTpr == 32) * (int)sizeof(typename Weight<T, kTpr == 32>::type);
+    if (kMost > 40 * 1024) {
+        static std::atomic<unsigned long long> done{0};
+        const cudaError_t e = allow_shared(kern, kMost, done);
         if (e != cudaSuccess) return e;
     }
     // as many blocks as are resident at once, so that each walks its rows;
@@ -826,8 +830,11 @@ cudaError_t backward(const Args &a, cudaStream_t s) {
     auto *kernel = norm_backward_kernel<T, V, kOwn, kThreads, kShared, kAhead, kPost, kPre>;
     const size_t smem = kShared ? 5 * sizeof(float) * (size_t)a.hidden
                         : staged<T, V>(kAhead, kShared) ? (size_t)2 * 4 * (kOwn / V) * 16 * backward_threads(a.hidden, V) : 0;
-    if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t kMost = kShared ? 5 * sizeof(float) * (size_t)kMaxHidden
+                             : staged<T, V>(kAhead, kShared) ? (size_t)2 * 4 * (kOwn / V) * 16 * kThreads : 0;
+    if (kMost > 40 * 1024) {
+        static std::atomic<unsigned long long> done{0};
+        const cudaError_t e = allow_shared(kernel, kMost, done);
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(kernel, dim3(a.blocks), dim3(backward_threads(a.hidden, V)), smem, s, a);
