@@ -69,6 +69,7 @@ struct Call {
     const int32_t *bucket;          // [2N-1]
     const int32_t *lists;           // [BH][cap] or null (every block)
     unsigned int *status;
+    int expire;                     // test hook: each block's first wait gives up at once
     // workspace
     uint32_t *valid;                // [B][nbr] valid tokens of each block
     float *vec;                     // [H][2*nbr*32] bias; j - i at index j - i + nbr*32

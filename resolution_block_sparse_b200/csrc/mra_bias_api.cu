@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <vector>
 
 #include "mra.h"
@@ -169,6 +170,10 @@ int prepare_call(const void *const *tensors, int n, const float *key_mask, const
     c->table = bias_table;
     c->bucket = bucket;
     c->lists = block_idx;
+    // MRA_TEST_EXPIRE_WAIT=1 (read at every call): the first wait of every block
+    // of the kernels that wait reports expiry without waiting, to test the way out
+    const char *expire = getenv("MRA_TEST_EXPIRE_WAIT");
+    c->expire = expire && expire[0] == '1' ? 1 : 0;
     return MRA_OK;
 }
 

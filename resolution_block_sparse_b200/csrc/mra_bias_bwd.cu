@@ -169,7 +169,7 @@ row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
         if (!kDelta && stat) ndelta[i] = stat[kTokens + g + 8 * i];
     }
 
-    bool ok = guarded_wait(&s.ring.first, 0, abort, c.status);
+    bool ok = first_wait(&s.ring.first, abort, c);
     const Lane<D> at(lane);
     unsigned qa[1][D / 16][4], ga[1][D / 16][4];
     load_a<D>(qa[0], s.q[0], wrow, at);
@@ -189,7 +189,7 @@ row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
             if (guarded_wait(&s.ring.empty[u % kStages], (u / kStages) & 1, abort, c.status)) fill(u + kStages);
         }
         __syncwarp();
-        ok = guarded_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
+        ok = warp_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
         if (!ok) break;
         const int entry = s.info.entry[t];
         if ((entry >> (kMemberShift + member)) & 1) {
@@ -332,11 +332,7 @@ row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
         if (ok && write)
             store_rows<D>(s.q[0], wrow, acc[0], c.scale, c.scale, dq + ((size_t)it.bh * c.N + qpos) * D, c.N - qpos, lane);
     }
-    if (*abort) {
-        __syncthreads();
-        if (tid == 0) ring_drain(s.ring);
-        __syncthreads();
-    }
+    ring_end(s.ring);
 }
 
 // ---------------------------------------------------------------- columns: dK, dV
@@ -394,7 +390,7 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
     const float *vec = c.vec + ((size_t)h * 2 + 1) * c.nbr * kTokens;
     volatile int *abort = &s.ring.abort;
 
-    bool ok = guarded_wait(&s.ring.first, 0, abort, c.status);
+    bool ok = first_wait(&s.ring.first, abort, c);
     const Lane<D> at(lane);
     unsigned ka[1][D / 16][4], va[1][D / 16][4];
     load_a<D>(ka[0], s.kv[0], wrow, at);
@@ -412,7 +408,7 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
             if (guarded_wait(&s.ring.empty[u % kStages], (u / kStages) & 1, abort, c.status)) fill(u + kStages);
         }
         __syncwarp();
-        ok = guarded_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
+        ok = warp_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
         if (!ok) break;
         const int entry = s.info.entry[t];
         if ((entry >> (kMemberShift + member)) & 1) {
@@ -503,11 +499,7 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
         store_rows<D>(s.kv[0], wrow, ak[0], c.scale, c.scale, dk + at, c.N - kpos, lane);
         store_rows<D>(s.kv[1], wrow, av[0], 1.0f, 1.0f, dv + at, c.N - kpos, lane);
     }
-    if (*abort) {
-        __syncthreads();
-        if (tid == 0) ring_drain(s.ring);
-        __syncthreads();
-    }
+    ring_end(s.ring);
 }
 
 template <int D>

@@ -91,7 +91,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                                : c.vec + ((size_t)h * 2 + 1) * c.nbr * kTokens;
     volatile int *abort = &s.ring.abort;
 
-    bool ok = guarded_wait(&s.ring.first, 0, abort, c.status);
+    bool ok = first_wait(&s.ring.first, abort, c);
     unsigned qa[2][D / 16][4];
     const Lane<D> at(lane);
     load_a<D>(qa[0], s.q, warp * 32, at);
@@ -117,7 +117,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         __syncwarp();
         // every warp waits for every block, so that none releases a stage twice
         // before the others have released it once
-        ok = guarded_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
+        ok = warp_wait(&s.ring.full[sg], (t / kStages) & 1, abort, c.status);
         if (!ok) break;
         const int entry = s.info.entry[t];
         if ((entry >> (kMemberShift + warp)) & 1) {
@@ -265,11 +265,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                           c.N - qpos - 16 * i, lane);
         }
     }
-    if (*abort) {
-        __syncthreads();
-        if (tid == 0) ring_drain(s.ring);
-        __syncthreads();
-    }
+    ring_end(s.ring);
 }
 
 template <int D, int kRows, bool kDirect>

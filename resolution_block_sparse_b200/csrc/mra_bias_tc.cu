@@ -53,7 +53,6 @@
 // copies and products in flight are waited for (bounded) and tensor memory is
 // freed.
 #include <algorithm>
-#include <cstdlib>
 
 #include "mra_bias_direct.cuh"
 #include "mra_bias_warp.cuh"
@@ -173,7 +172,6 @@ struct TcPtrs {
     const float *lse;           // kDelta
     __nv_bfloat16 *out, *out2;  // O; dQ; dK, dV
     float *lse_out;
-    int expire;                 // test hook: the first wait gives up at once
 };
 
 // x (scores of this thread's row) with scale, bias and masks:
@@ -605,11 +603,11 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
             bool ok = true;
             for (int st = 0; ok && st < steps; ++st, ++t) {
                 const int sg = t % kStages, buf = t % kBuffers, i = st * S::stack + half;
-                if (g.expire && t == 0) {
+                if (c.expire && t == 0) {
                     *abort = 1;
                     atomicOr(c.status, kDevTimeout);
                 }
-                ok = !(g.expire && t == 0) && wait_warp(&s.scores[buf], (t / kBuffers) & 1);
+                ok = !(c.expire && t == 0) && wait_warp(&s.scores[buf], (t / kBuffers) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const int entry = i < it.count ? x_item.info.entry[i] : 0;
@@ -936,17 +934,13 @@ struct Maps {
 };
 
 template <int kMode, bool kDirect>
-cudaError_t launch(const Call &c, const Maps &m, TcPtrs g, cudaStream_t s) {
+cudaError_t launch(const Call &c, const Maps &m, const TcPtrs &g, cudaStream_t s) {
     const size_t bin = kMode == kRows ? kSoftWarps * sizeof(float) : 0;
     const size_t fixed = sizeof(TcSmem<kMode>) + 1024 + (kDirect ? sizeof(Window) : 0), smem = fixed + bin * c.buckets;
     auto *kern = tc_kernel<kMode, kDirect>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_shared(kern, fixed + bin * kMaxBuckets, done);
     if (e != cudaSuccess) return e;
-    // MRA_TEST_EXPIRE_WAIT=1 (read at every launch): the first wait of every
-    // block's softmax reports expiry without waiting, to test the way out
-    const char *expire = getenv("MRA_TEST_EXPIRE_WAIT");
-    g.expire = expire && expire[0] == '1' ? 1 : 0;
     const int grid = kDirect ? c.BH * c.groups : std::min(kMode == kCols ? c.col_items : c.row_items, 2 * device_sm_count());
     return launch_dependent(kern, dim3(grid), dim3(kTcThreads), smem, s, m.a1, m.a2, m.b1, m.b2, c, g);
 }
@@ -955,7 +949,7 @@ cudaError_t launch(const Call &c, const Maps &m, TcPtrs g, cudaStream_t s) {
 
 cudaError_t launch_forward_tc(const Call &c, const void *q, const void *k, const void *v, void *out, float *lse,
                               cudaStream_t s) {
-    const TcPtrs g{nullptr, static_cast<__nv_bfloat16 *>(out), nullptr, lse, 0};
+    const TcPtrs g{nullptr, static_cast<__nv_bfloat16 *>(out), nullptr, lse};
     Maps m;
     if (!make_head_map(&m.a1, q, c.BH, c.N, kD, kTileRows) || !make_head_map(&m.b1, k, c.BH, c.N, kD, kTokens) ||
         !make_head_map(&m.b2, v, c.BH, c.N, kD, kTokens))
@@ -976,9 +970,9 @@ cudaError_t launch_backward_tc(const Call &c, const void *q, const void *k, cons
             !make_head_map(block[i], by_rows[i], c.BH, c.N, kD, kTokens))
             return cudaErrorInvalidValue;
     *launches += 3;
-    cudaError_t e = launch<kDelta, false>(c, rows, TcPtrs{lse, nullptr, nullptr, nullptr, 0}, s);
-    if (e == cudaSuccess) e = launch<kRows, false>(c, rows, TcPtrs{nullptr, oq, nullptr, nullptr, 0}, s);
-    if (e == cudaSuccess) e = launch<kCols, false>(c, cols, TcPtrs{nullptr, ok, ov, nullptr, 0}, s);
+    cudaError_t e = launch<kDelta, false>(c, rows, TcPtrs{lse, nullptr, nullptr, nullptr}, s);
+    if (e == cudaSuccess) e = launch<kRows, false>(c, rows, TcPtrs{nullptr, oq, nullptr, nullptr}, s);
+    if (e == cudaSuccess) e = launch<kCols, false>(c, cols, TcPtrs{nullptr, ok, ov, nullptr}, s);
     return e;
 }
 

@@ -98,10 +98,27 @@ __device__ __forceinline__ bool guarded_wait(unsigned long long *bar, uint32_t p
     return false;
 }
 
-// After a stop: no copy of this block may land after its shared memory is
-// given up.  One thread waits (bounded) for every stage it filled.
+// The same answer for the whole warp, whose collective instructions follow.
+__device__ __forceinline__ bool warp_wait(unsigned long long *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+    return __all_sync(0xffffffffu, guarded_wait(bar, parity, abort, status));
+}
+
+// A block's first wait; with the test hook it gives up at once.
+__device__ __forceinline__ bool first_wait(unsigned long long *bar, volatile int *abort, const Call &c) {
+    if (c.expire) {
+        *abort = 1;
+        atomicOr(c.status, kDevTimeout);
+        return false;
+    }
+    return warp_wait(bar, 0, abort, c.status);
+}
+
+// The block's end, for all of its threads.  After a stop no copy of the block
+// may land after its shared memory is given up: one thread waits (bounded) for
+// every stage filled.
 template <int kStages>
-__device__ __forceinline__ void ring_drain(Ring<kStages> &r) {
+__device__ __forceinline__ void ring_end(Ring<kStages> &r) {
+    if (!__syncthreads_or(*(volatile int *)&r.abort) || threadIdx.x != 0) return;
     mbar_wait(saddr(&r.first), 0);
     for (int t = max(0, r.issued - kStages); t < r.issued; ++t)
         mbar_wait(saddr(&r.full[t % kStages]), (t / kStages) & 1);
