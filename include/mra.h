@@ -282,8 +282,15 @@ MRA_API int mra_bigbird_block_list(int N, int block_size, int num_random, const 
  *     is smaller.  Its contents need not be kept between calls.
  * The backward pass takes the forward's lse and the gradient dout of out;
  * dq, dk, dv ([B][H][N][D]) and dbias_table ([num_buckets][H]) are written in
- * the element type of q.  Sums are fp32, in a fixed order: equal calls give
- * equal bits.  The first call on a device must come before any stream
+ * the element type of q.  Arithmetic: scores, softmax statistics, delta and all
+ * sums are fp32, in a fixed order: equal calls give equal bits.  With fp32
+ * tensors the products are fp32 too.  With bf16 tensors the weights enter their
+ * products in bf16: P of the forward pass rounded once, so that out has about
+ * sqrt(2) times the error of the rounded exact result; P and dS of the backward
+ * pass rounded once, with the same effect on dq, dk and dv, in the kernels for
+ * heads of 64 with at least 68 listed blocks per SM over all heads, and in two
+ * bf16 pieces otherwise (heads of 32 always), where the results' own rounding
+ * is all that counts.  The bias gradient is an fp32 sum of fp32 terms.  The first call on a device must come before any stream
  * capture.  Asynchronous on `stream`; returns an mra_status value. */
 MRA_API size_t mra_blocksparse_attention_bias_workspace(int B, int H, int N, int D, int cap_sel, int num_buckets,
                                                         int dtype, int backward);
@@ -368,8 +375,9 @@ MRA_API int mra_qkv_projection(const void *x, const void *w_qkv, const float *b_
  * The backward pass takes the gradients dx_out of x' and dy of y (NULL: that
  * output took no part, dy not NULL exactly with MRA_NORM_PRE) and the
  * forward's stats, and writes dx, dh (NULL exactly when h is) and, where not
- * NULL, dgate, dpost_w, dpost_b, dpre_w, dpre_b (in the element type; sums in
- * fp32 in a fixed order, so equal calls give equal bits).  workspace: DEVICE,
+ * NULL, dgate, dpost_w, dpost_b, dpre_w, dpre_b (in the element type).  All
+ * arithmetic is fp32, sums over rows and columns in a fixed order, so equal
+ * calls give equal bits.  workspace: DEVICE,
  * 16-byte aligned, mra_residual_norm_workspace(rows, hidden) bytes;
  * MRA_ERR_TOO_LARGE when workspace_bytes is less.  No state is kept in the
  * library: calls may overlap, each with its own workspace.  Asynchronous on

@@ -35,9 +35,6 @@ constexpr int kGroup = 2;               // block rows (columns) per work item, b
 constexpr int kMaxGroup = 4;            // forward in bf16: two or four
 constexpr float kExcluded = -1e30f;     // table values at or below exclude the pair
 constexpr int kMaxBuckets = 1024;
-// dq, dk, dv of at most this many values have their weights P and dS in two bf16
-// pieces (mra_bias_bwd.cu)
-constexpr long long kResidual = 1 << 17;
 constexpr int kMaxChunk = 64;           // union blocks per work item, at most
 constexpr float kLog2e = 1.4426950408889634f;
 // counters of a call, for rows and for columns: whole groups, items of split
@@ -85,7 +82,6 @@ struct Call {
     // backward
     float *rowstat;                 // [BH][nbr][2][32] minus lse, minus delta
     float *bins;                    // [BH*groups][buckets] bias gradient of each group
-    int residual;                   // warp-level kernels: weights in two bf16 pieces
     void *dtable;                   // [buckets][H], element type of q
     int table_bf16;
 };

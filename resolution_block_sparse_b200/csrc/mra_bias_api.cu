@@ -37,19 +37,18 @@ int plan(int B, int H, int N, int D, int cap, bool lists, int buckets, int dtype
     // tcgen05 kernels (bf16, heads of 64) or warp-level ones.  The first take four
     // block rows an item, pay for the union of their lists and need more work to
     // fill the GPU; listed: the blocks of all heads' lists.  Measured (us, warp-level
-    // against tcgen05; B x H, N, share listed):
-    //  backward, all blocks: 4x12, 512: 89 / 72; 1x12, 1024: 95 / 85; 1x2, 2048:
-    //   71 / 86; 1x12, 512: 45 / 58
-    //  backward, lists: 2x12, 4096, BigBird (15 %): 357 / 260, 9 %: 294 / 268, 6 %:
-    //   215 / 212, 3 %: 138 / 156; 2x12, 1024, 69 %: 144 / 123, 24 %: 79 / 79; 1x2,
-    //   4096, 22 %: 95 / 102
+    // against tcgen05; B x H, N, blocks a row; in brackets listed blocks per SM):
+    //  backward (with the forward), all blocks: 4x12, 512 [83]: 115 / 87; 1x3, 2048
+    //   [83]: 130 / 119; 1x8, 1024 [55]: 101 / 95; 1x2, 2048 [55]: 104 / 110; 2x12,
+    //   512 [42]: 80 / 78; 1x12, 512 [21]: 58 / 67
+    //  backward, lists: 2x12, 4096, 8 [166]: 293 / 262, 4 [83]: 192 / 190; 1x4, 4096,
+    //   28 [97]: 185 / 162; 1x2, 4096, 28 [48]: 124 / 123; 2x12, 1024, 8 [42]: 111 / 102
     //  forward (heads of 64 have the tcgen05 kernel alone), when both were there:
     //   2x12, 4096, all blocks: 453 / 236, BigBird 91 / 77, random lists of 3 to
     //   12 % within 10 % of each other
     const long long all = (long long)c->nbr * c->nbr, listed = (long long)B * H * (lists ? cap : all);
     const int sms = device_sm_count();
-    c->tc = dtype == MRA_DTYPE_BF16 && D == 64 &&
-            (!backward || listed >= (lists ? 110LL : 68LL) * sms);
+    c->tc = dtype == MRA_DTYPE_BF16 && D == 64 && (!backward || listed >= 68LL * sms);
     // The warp-level forward kernel (heads of 32) takes four rows an item where
     // every second block or more is listed (their union is then little longer
     // than one row, and the traffic from L2 halves again), else two.
@@ -251,7 +250,6 @@ int mra_blocksparse_attention_bias_bwd(const void *q, const void *k, const void 
     int launches = 0;
     c.dtable = dbias_table;
     c.table_bf16 = bf16 ? 1 : 0;
-    c.residual = (long long)c.BH * N * D <= bias::kResidual ? 1 : 0;
     cudaError_t e = bias::launch_prepare(c, bf16, true, stream, &launches);
     if (e == cudaSuccess)
         e = c.tc ? bias::launch_backward_tc(c, q, k, v, lse, dout, dq, dk, dv, stream, &launches)

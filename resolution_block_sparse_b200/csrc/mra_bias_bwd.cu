@@ -81,13 +81,13 @@ __device__ __forceinline__ void bin_diagonals(const float (&ds)[4][4], float *ti
     bin_runs(s1, b1, bins, distinct, lane);
 }
 
-// What the rounding of an operand to bf16 leaves.  A result's rounding and that of
-// its weights are independent and of one size, so that its error is sqrt(2) times
-// that of the rounded exact result, give or take what its number of values
-// averages; small calls, which wait for latency and not for products, take the
-// rest in a second product (1 x 4 heads of 256, backward: 31.5 to 32.8 us and the
-// errors of dq, dk and dv from 1.4 times the rounded exact results' to 1.0; 1 x 2
-// heads of 2048, which do wait for products: 68 to 81).
+// What the rounding of an operand to bf16 leaves.  P and dS enter their products
+// in two bf16 pieces.  A weight's rounding and its result's are independent and of
+// one size, so that weights rounded once give dq, dk and dv sqrt(2) times the
+// error of the rounded exact result; with the rest in a second product it is that
+// of the rounding alone, and costs 0 to 9 % (forward and backward, rounded once / in
+// two pieces: 1 x 4 heads of 256 of 64 42.8 / 42.8 us, 1 x 2 of 2048 97.7 / 104; heads
+// of 32: 8 x 12 of 512 120 / 127, 2 x 12 of 4096 1697 / 1850, BigBird 334 / 357).
 __device__ __forceinline__ float2 residual(float2 v) {
     const unsigned h = mma::pack_bf16(v.x, v.y);
     return make_float2(v.x - __uint_as_float(h << 16), v.y - __uint_as_float(h & 0xffff0000u));
@@ -232,14 +232,12 @@ row_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUten
                 }
             }
             if (!kDelta) {
-                mul_ab<D, 1>(acc, w, s.kv[sg][0], at, lane, kv);
-                if (c.residual) {
+                unsigned low[2][4];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) put_operand(w[0], n, k, residual(pair_of(x[0], n, k)));
-                    mul_ab<D, 1>(acc, w, s.kv[sg][0], at, lane, kv);
-                }
+                    for (int k = 0; k < 2; ++k) put_operand(low, n, k, residual(pair_of(x[0], n, k)));
+                mul_ab_pieces<D>(acc[0], w[0], low, s.kv[sg][0], at, lane, kv);
                 const int tb = s.bucket[member][t];
                 if (tb >= 0) {
                     if (tb != bin.cur) {
@@ -430,7 +428,8 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
                             if (!pair_on(keys_on, qv, n, e, lane)) dp[0][n][e] = 0.0f;
                 }
             }
-            unsigned wp[1][2][4], ws[1][2][4];
+            // P in two pieces, then dS over them
+            unsigned high[2][4], low[2][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 nl = *reinterpret_cast<const float2 *>(&s.stat[sg][0][8 * n + 2 * (lane & 3)]);
@@ -438,25 +437,23 @@ __device__ __forceinline__ void col_item(const CUtensorMap &tq, const CUtensorMa
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float2 p = weight2(pair_of(x[0], n, k), sc, add, nl);
-                    put_operand(wp[0], n, k, p);
-                    put_operand(ws[0], n, k, mul2(p, add2(pair_of(dp[0], n, k), nd)));
+                    const float2 ds = mul2(p, add2(pair_of(dp[0], n, k), nd));
+                    put_operand(high, n, k, p);
+                    put_operand(low, n, k, residual(p));
+                    x[0][n][2 * k] = ds.x;
+                    x[0][n][2 * k + 1] = ds.y;
                 }
             }
-            mul_ab_two<D>(av[0], ak[0], wp[0], ws[0], s.qg[sg][1], s.qg[sg][0], at, lane, qv);
-            if (c.residual) {
+            mul_ab_pieces<D>(av[0], high, low, s.qg[sg][1], at, lane, qv);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 nl = *reinterpret_cast<const float2 *>(&s.stat[sg][0][8 * n + 2 * (lane & 3)]);
-                    const float2 nd = *reinterpret_cast<const float2 *>(&s.stat[sg][1][8 * n + 2 * (lane & 3)]);
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 p = weight2(pair_of(x[0], n, k), sc, add, nl);
-                        put_operand(wp[0], n, k, residual(p));
-                        put_operand(ws[0], n, k, residual(mul2(p, add2(pair_of(dp[0], n, k), nd))));
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const float2 ds = pair_of(x[0], n, k);
+                    put_operand(high, n, k, ds);
+                    put_operand(low, n, k, residual(ds));
                 }
-                mul_ab_two<D>(av[0], ak[0], wp[0], ws[0], s.qg[sg][1], s.qg[sg][0], at, lane, qv);
-            }
+            mul_ab_pieces<D>(ak[0], high, low, s.qg[sg][0], at, lane, qv);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(saddr(&s.ring.empty[sg]));

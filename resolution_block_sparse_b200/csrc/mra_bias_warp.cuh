@@ -270,46 +270,36 @@ __device__ __forceinline__ void mul_ab(float (&acc)[kM][D / 8][4], const unsigne
     }
 }
 
-// Two such products, acc1 += W1 . tile1 and acc2 += W2 . tile2, in step.
+// acc += (high + low) . tile: weights in two bf16 pieces.
 template <int D>
-__device__ __forceinline__ void mul_ab_two(float (&acc1)[D / 8][4], float (&acc2)[D / 8][4], const unsigned (&w1)[2][4],
-                                           const unsigned (&w2)[2][4], const __nv_bfloat16 *tile1,
-                                           const __nv_bfloat16 *tile2, const Lane<D> &at, int lane, uint32_t keep) {
-    const uint32_t b1 = mma::smem_u32(tile1) + at.tall, b2 = mma::smem_u32(tile2) + at.tall;
+__device__ __forceinline__ void mul_ab_pieces(float (&acc)[D / 8][4], const unsigned (&high)[2][4], const unsigned (&low)[2][4],
+                                              const __nv_bfloat16 *tile, const Lane<D> &at, int lane, uint32_t keep) {
+    const uint32_t base = mma::smem_u32(tile) + at.tall;
     const Keep rows(keep, lane);
     const bool masked = keep != 0xffffffffu;
     constexpr int kSteps = D / 8;
-    unsigned r[2][2][4];
-    ldsm_t<0>(r[0][0], b1);
-    ldsm_t<0>(r[0][1], b2);
+    unsigned r[2][4];
+    ldsm_t<0>(r[0], base);
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
         const int s = n & 1, kk = n / (kSteps / 2), t = n % (kSteps / 2) * 2;
         if (n + 1 < kSteps) {
             const int k1 = (n + 1) / (kSteps / 2), t1 = (n + 1) % (kSteps / 2) * 2;
-            if (k1 == 0) {
-                ldsm_t<0>(r[s ^ 1][0], b1 ^ (t1 << 4));
-                ldsm_t<0>(r[s ^ 1][1], b2 ^ (t1 << 4));
-            } else {
-                ldsm_t<16 * D * 2>(r[s ^ 1][0], b1 ^ (t1 << 4));
-                ldsm_t<16 * D * 2>(r[s ^ 1][1], b2 ^ (t1 << 4));
-            }
+            if (k1 == 0) ldsm_t<0>(r[s ^ 1], base ^ (t1 << 4));
+            else ldsm_t<16 * D * 2>(r[s ^ 1], base ^ (t1 << 4));
         }
-        if (masked) {
-            rows.apply(r[s][0], kk);
-            rows.apply(r[s][1], kk);
-        }
-        mma16816(acc1[t], w1[kk], r[s][0][0], r[s][0][1]);
-        mma16816(acc1[t + 1], w1[kk], r[s][0][2], r[s][0][3]);
-        mma16816(acc2[t], w2[kk], r[s][1][0], r[s][1][1]);
-        mma16816(acc2[t + 1], w2[kk], r[s][1][2], r[s][1][3]);
+        if (masked) rows.apply(r[s], kk);
+        mma16816(acc[t], high[kk], r[s][0], r[s][1]);
+        mma16816(acc[t + 1], high[kk], r[s][2], r[s][3]);
+        mma16816(acc[t], low[kk], r[s][0], r[s][1]);
+        mma16816(acc[t + 1], low[kk], r[s][2], r[s][3]);
     }
 }
 
 // Two neighbouring elements of a score tile, and their place in the A operand
-// of mul_ab.  The weights (and dS) enter the tensor cores as bf16: their
-// rounding is one half step of the operand type, as large as that of the
-// result's own type.
+// of mul_ab.  The weights enter the tensor cores as bf16: rounded once forward,
+// a half step of the operand type, as large as that of the result's own type;
+// in two pieces backward (mra_bias_bwd.cu).
 __device__ __forceinline__ float2 pair_of(const float (&x)[4][4], int n, int k) {
     return make_float2(x[n][2 * k], x[n][2 * k + 1]);
 }
