@@ -118,12 +118,15 @@ __device__ __forceinline__ bool take_item(const Item *items, const int *counters
     *it = items[i < split ? i : capacity - 1 - (i - split)];
     return it->bh >= 0;
 }
-// lse of a row from its reference m (natural units) and the sum of its
-// weights against it.  Where one key holds all the weight that sum is 1 but for
-// the rounding of the exponent; lse is then the key's score itself, so that the
-// backward pass finds its weight to be exactly 1 and its dS exactly 0.
-__device__ __forceinline__ float row_lse(float m, float sum) {
-    return fabsf(sum - 1.0f) <= 2.4e-7f * fmaxf(1.0f, fabsf(m)) ? m : m + logf(sum);
+// The weight that exp2(x * (sc log2 e) + (add - m) log2 e) gives the score m = x *
+// sc + add itself: 1 but for the exponent's rounding.  Where a row's reference
+// moves to m, its sum is given 1 minus that: the reference then counts exactly 1,
+// so that a row of one key has lse m and the backward pass finds its weight to be
+// exactly 1 and its dS exactly 0, and no other key's weight is lost.
+__device__ __forceinline__ float reference_rest(float x, float sc, float add, float m) {
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(w) : "f"(fmaf(x, sc * kLog2e, (add - m) * kLog2e)));
+    return 1.0f - w;
 }
 
 __device__ __forceinline__ int item_chunk(const Item &it) { return it.chunk & 0xffff; }

@@ -498,7 +498,7 @@ __device__ __forceinline__ void f32_item(const Call &c, const Ptrs &g, unsigned 
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) acc[i][k] = 0.0f;
             if (g.lse_out && tx == 0 && n < c.N)
-                g.lse_out[(size_t)it.bh * c.N + n] = live ? row_lse(m[i], l[i]) : -INFINITY;
+                g.lse_out[(size_t)it.bh * c.N + n] = live ? m[i] + logf(l[i]) : -INFINITY;
         }
     }
     write_rows<D>(g.out + head + (size_t)pos * D, acc, f, c.N - pos, ty, tx);

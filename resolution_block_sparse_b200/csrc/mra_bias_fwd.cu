@@ -135,7 +135,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 sc = 1.0f;
                 add = 0.0f;
             }
-            float mx[2][2];
+            float top[2][2];      // before scale and bias
             bool move = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -144,19 +144,21 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     float y = fmaxf(x[i][0][2 * k], x[i][0][2 * k + 1]);
 #pragma unroll
                     for (int n = 1; n < 4; ++n) y = fmaxf(fmaxf(y, x[i][n][2 * k]), x[i][n][2 * k + 1]);
-                    mx[i][k] = fmaf(y, sc, add);
-                    move = move || mx[i][k] > m[i][k] + kMove || (m[i][k] == -INFINITY && mx[i][k] > m[i][k]);
+                    const float mx = fmaf(y, sc, add);
+                    top[i][k] = y;
+                    move = move || mx > m[i][k] + kMove || (m[i][k] == -INFINITY && mx > m[i][k]);
                 }
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float y = quad_max(mx[i][k]);
+                        const float x_top = quad_max(top[i][k]), y = fmaf(x_top, sc, add);
                         if (y > m[i][k]) {
                             const float f = fast_exp2((m[i][k] - y) * kLog2e);
                             m[i][k] = y;
                             l[i][k] = mul2(l[i][k], both(f));
+                            if ((lane & 3) == 0) l[i][k].x += reference_rest(x_top, sc, add, y);
 #pragma unroll
                             for (int n = 0; n < D / 8; ++n) {
                                 o[i][n][2 * k] *= f;
@@ -259,7 +261,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     for (int t = 0; t < D / 8; ++t) o[i][t][2 * k] = o[i][t][2 * k + 1] = 0.0f;
                 }
                 if (lse && (lane & 3) == 0 && qpos + n < c.N)
-                    lse[(size_t)it.bh * c.N + qpos + n] = live ? row_lse(m[i][k], sum[i][k]) : -INFINITY;
+                    lse[(size_t)it.bh * c.N + qpos + n] = live ? m[i][k] + logf(sum[i][k]) : -INFINITY;
             }
             store_rows<D>(s.q, warp * 32 + 16 * i, o[i], f[0], f[1], out + ((size_t)it.bh * c.N + qpos + 16 * i) * D,
                           c.N - qpos - 16 * i, lane);

@@ -631,13 +631,14 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                                       max3(x[9], x[10], x[11])};
 #pragma unroll
                         for (int e = 12; e < 32; e += 2) y[(e >> 1) & 3] = max3(y[(e >> 1) & 3], x[e], x[e + 1]);
-                        const float mx = fmaf(fmaxf(max3(y[0], y[1], y[2]), y[3]), sc, add);
+                        const float top = fmaxf(max3(y[0], y[1], y[2]), y[3]), mx = fmaf(top, sc, add);
                         const bool move = mx > m + kMove || (m == -INFINITY && mx > m);
                         if (__any_sync(0xffffffffu, move)) {
                             const float f = move ? fast_exp2((m - mx) * kLog2e) : 1.0f;
                             if (move) m = mx;
                             sum[0] = mul2(sum[0], both(f));
                             sum[1] = mul2(sum[1], both(f));
+                            if (move) sum[0].x += reference_rest(top, sc, add, mx);
                             if (st > 0) {
                                 // the output so far, once the last step's products are in
                                 wait_warp(&s.empty[(t - 1) % kStages], ((t - 1) / kStages) & 1);
@@ -886,7 +887,7 @@ tc_kernel(const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUten
                             for (int e = 0; e < kVals; ++e) o[e] = 0.0f;
                         }
                         if (g.lse_out && half == 0)
-                            g.lse_out[(size_t)it.bh * c.N + pos] = live ? row_lse(m, total) : -INFINITY;
+                            g.lse_out[(size_t)it.bh * c.N + pos] = live ? m + logf(total) : -INFINITY;
                     }
                     const bool wide = ((uintptr_t)(cols && half == 1 ? g.out2 : g.out) & 31) == 0;
                     __nv_bfloat16 *dst = (cols && half == 1 ? g.out2 : g.out) + ((size_t)it.bh * c.N + pos) * kD +

@@ -39,3 +39,40 @@ def test_error_norms(name):
     top = 1.1 if name in WARP else 1.5
     assert r["out"] <= 1.5 and r["dtable"] <= 1.1, r
     assert max(r["dq"], r["dk"], r["dv"]) <= top, r
+
+
+@pytest.mark.parametrize("N", [2, 70, 1100])
+@pytest.mark.parametrize("D,dtype,top,second", [(D, t, *x) for D in (64, 32) for t in (BF16, torch.float32)
+                                                for x in ((30.0, 18.125), (1000.0, 991.6))
+                                                if t != BF16 or x[0] == 30.0])      # (991.6 is no bf16 number)
+def test_lse_of_large_scores(N, D, dtype, top, second):
+    """A key of score `top` and neighbours of score `second`, whose small weights
+    count: the scores are the table's values, exact in the type, so that the lse
+    is off by its own rounding (half a step of `top`) and by a hundredth of it
+    for the weights' and the logarithm's."""
+    p = Problem(1, 2, N, D, dtype, 7, nb=4)
+    p.q.zero_()
+    p.table.fill_(0.0)
+    p.table[0], p.table[1] = top, second
+    p.bucket.fill_(-1)
+    p.bucket[N - 1] = 0
+    p.bucket[N - 2] = p.bucket[N] = 1
+    got = p.forward()["lse"].double()
+    n = torch.full((N,), 2.0, dtype=torch.float64, device="cuda")
+    n[0] = n[-1] = 1.0
+    want = top + torch.log1p(n * torch.exp(p.table[1, 0].double() - top))
+    step = 2.0 ** (4 - 23) if top == 30.0 else 2.0 ** (9 - 23)
+    assert float((got - want).abs().max()) <= 0.51 * step
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (32, BF16), (64, torch.float32)])
+@pytest.mark.parametrize("spread", [1.0, 8.0, 60.0])
+def test_rows_of_one_key_with_large_scores(D, dtype, spread):
+    """The first rows of causal heads, with scores up to thousands: weight 1, no
+    gradient of the scores, lse the score itself."""
+    p = Problem(4, 8, 140, D, dtype, 19, causal=True, spread=spread)
+    got = p.both()
+    assert torch.equal(got["out"][:, :, 0], p.v[:, :, 0]) and float(got["dq"][:, :, 0].abs().max()) == 0.0
+    s = (p.q[:, :, 0].double() * p.k[:, :, 0].double()).sum(-1) * p.scale + p.table[p.bucket[139].long()].double()
+    size = (p.q[:, :, 0].double() * p.k[:, :, 0].double()).abs().sum(-1) * p.scale + 8.0
+    assert bool(((got["lse"][:, :, 0].double() - s).abs() <= 2.0 ** -20 * size).all())
