@@ -236,12 +236,34 @@ struct PhaseScope {
     }
 };
 
+// Clears the status word before it returns: cudaMemset alone waits in the legacy
+// stream, behind whatever is queued there, and could clear what a kernel on a
+// non-blocking stream has raised meanwhile.
+int clear_status(unsigned int *word, size_t bytes) {
+    if (cudaMemset(word, 0, bytes) != cudaSuccess) return MRA_ERR_CUDA;
+    return cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess ? MRA_OK : MRA_ERR_CUDA;
+}
+
+// The device's status word, made on its first call.
+int ensure_status(DeviceCtx &ctx) {
+    if (ctx.status) return MRA_OK;
+    unsigned int *word = nullptr;
+    if (cudaMalloc(&word, 256) != cudaSuccess) {
+        cudaGetLastError();
+        return MRA_ERR_ALLOC;
+    }
+    const int rc = clear_status(word, 256);
+    if (rc != MRA_OK) {
+        cudaFree(word);
+        return rc;
+    }
+    ctx.status = word;
+    return MRA_OK;
+}
+
 int ensure_workspace(int dev, const Problem &p, Workspace *w) {
     DeviceCtx &ctx = g_dev[dev];
-    if (!ctx.status) {
-        if (cudaMalloc(&ctx.status, 256) != cudaSuccess) return MRA_ERR_ALLOC;
-        if (cudaMemset(ctx.status, 0, 256) != cudaSuccess) return MRA_ERR_CUDA;
-    }
+    if (const int failed = ensure_status(ctx)) return failed;
     const size_t need = carve_workspace(p, nullptr, nullptr);
     if (need > ctx.ws_bytes) {
         // MRA_TEST_FAIL_ALLOC=1 (read at every growth) makes the growth fail
@@ -537,10 +559,7 @@ int current_status_word(unsigned int **word) {
     const int rc = current_device(&dev);
     if (rc != MRA_OK) return rc;
     DeviceCtx &ctx = g_dev[dev];
-    if (!ctx.status) {
-        if (cudaMalloc(&ctx.status, 256) != cudaSuccess) return MRA_ERR_ALLOC;
-        if (cudaMemset(ctx.status, 0, 256) != cudaSuccess) return MRA_ERR_CUDA;
-    }
+    if (const int failed = ensure_status(ctx)) return failed;
     *word = ctx.status;
     return MRA_OK;
 }
@@ -571,10 +590,7 @@ int mra_qkv_projection(const void *x, const void *w_qkv, const float *b_qkv, voi
     rc = current_device(&dev);
     if (rc != MRA_OK) return rc;
     DeviceCtx &ctx = g_dev[dev];
-    if (!ctx.status) {
-        if (cudaMalloc(&ctx.status, 256) != cudaSuccess) return MRA_ERR_ALLOC;
-        if (cudaMemset(ctx.status, 0, 256) != cudaSuccess) return MRA_ERR_CUDA;
-    }
+    if (const int failed = ensure_status(ctx)) return failed;
     MRA_TRY(launch_qkv_projection(x, w_qkv, b_qkv, qkv, B, N, hidden, H, ctx.status, stream));
     g_last_launches = 1;
     return MRA_OK;
@@ -757,7 +773,7 @@ int mra_get_device_status(cudaStream_t stream) {
     unsigned int word = 0;
     if (cudaMemcpy(&word, ctx.status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return -MRA_ERR_CUDA;
-    if (cudaMemset(ctx.status, 0, sizeof(word)) != cudaSuccess) return -MRA_ERR_CUDA;
+    if (clear_status(ctx.status, sizeof(word)) != MRA_OK) return -MRA_ERR_CUDA;
     return (int)word;
 }
 
