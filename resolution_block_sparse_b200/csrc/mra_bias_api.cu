@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
-#include <vector>
 
 #include "mra.h"
 #include "mra_bias.cuh"
@@ -176,26 +175,30 @@ int prepare_call(const void *const *tensors, int n, const float *key_mask, const
     return MRA_OK;
 }
 
-// n^K first^m >= max^m first^K in whole numbers (32-bit limbs).
-std::vector<uint32_t> power_product(uint32_t a, int ea, uint32_t b, int eb) {
-    std::vector<uint32_t> x{1};
-    auto times = [&x](uint32_t f) {
+// A whole number for n^K first^m >= max^m first^K, in 32-bit limbs: at most 512
+// factors below 2^31 and 512 of at most 512 (kMaxBuckets / 2), 656 limbs.  No
+// memory of its own: an exception must not leave a C entry.
+struct Whole {
+    int n = 1;
+    uint32_t limb[(bias::kMaxBuckets / 2) * (31 + 10) / 32 + 1] = {1};
+    void times(uint32_t f) {
         uint64_t carry = 0;
-        for (uint32_t &limb : x) {
-            carry += (uint64_t)limb * f;
-            limb = (uint32_t)carry;
+        for (int i = 0; i < n; ++i) {
+            carry += (uint64_t)limb[i] * f;
+            limb[i] = (uint32_t)carry;
             carry >>= 32;
         }
-        if (carry) x.push_back((uint32_t)carry);
-    };
-    for (int i = 0; i < ea; ++i) times(a);
-    for (int i = 0; i < eb; ++i) times(b);
-    return x;
-}
-bool at_least(const std::vector<uint32_t> &a, const std::vector<uint32_t> &b) {
-    if (a.size() != b.size()) return a.size() > b.size();
-    for (size_t i = a.size(); i-- > 0;)
-        if (a[i] != b[i]) return a[i] > b[i];
+        if (carry) limb[n++] = (uint32_t)carry;
+    }
+    Whole(uint32_t a, int ea, uint32_t b, int eb) {
+        for (int i = 0; i < ea; ++i) times(a);
+        for (int i = 0; i < eb; ++i) times(b);
+    }
+};
+bool at_least(const Whole &a, const Whole &b) {
+    if (a.n != b.n) return a.n > b.n;
+    for (int i = a.n; i-- > 0;)
+        if (a.limb[i] != b.limb[i]) return a.limb[i] > b.limb[i];
     return true;
 }
 
@@ -277,7 +280,7 @@ int mra_relative_buckets(int N, int num_buckets, int max_distance, int bidirecti
             // next to a border the whole-number comparison decides
             const int near = (int)std::lround(t);
             if (std::fabs(t - near) < 1e-6)
-                m = near == 0 || at_least(power_product(n, far, first, near), power_product(max_distance, near, first, far))
+                m = near == 0 || at_least(Whole(n, far, first, near), Whole(max_distance, near, first, far))
                         ? near
                         : near - 1;
             b = std::min(first + m, per - 1);
