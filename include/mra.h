@@ -278,8 +278,9 @@ MRA_API int mra_bigbird_block_list(int N, int block_size, int num_random, const 
  *     and its gradient NaN.
  *   workspace: DEVICE, 256-byte aligned, at least as many bytes as
  *     mra_blocksparse_attention_bias_workspace says for the same sizes
- *     (cap_sel 0: block_idx NULL; backward 0 or 1); MRA_ERR_TOO_LARGE when it
- *     is smaller.  Its contents need not be kept between calls.
+ *     (cap_sel 0: block_idx NULL; backward 0 or 1) with the call's device
+ *     current (the size goes by its SMs); MRA_ERR_TOO_LARGE when it is
+ *     smaller.  Its contents need not be kept between calls.
  * The backward pass takes the forward's lse and the gradient dout of out;
  * dq, dk, dv ([B][H][N][D]) and dbias_table ([num_buckets][H]) are written in
  * the element type of q.  Arithmetic: scores, softmax statistics, delta and all
@@ -378,8 +379,9 @@ MRA_API int mra_qkv_projection(const void *x, const void *w_qkv, const float *b_
  * NULL, dgate, dpost_w, dpost_b, dpre_w, dpre_b (in the element type).  All
  * arithmetic is fp32, sums over rows and columns in a fixed order, so equal
  * calls give equal bits.  workspace: DEVICE,
- * 16-byte aligned, mra_residual_norm_workspace(rows, hidden) bytes;
- * MRA_ERR_TOO_LARGE when workspace_bytes is less.  No state is kept in the
+ * 16-byte aligned, mra_residual_norm_workspace(rows, hidden) bytes, asked for
+ * with the call's device current; MRA_ERR_TOO_LARGE when workspace_bytes is
+ * less.  No state is kept in the
  * library: calls may overlap, each with its own workspace.  Asynchronous on
  * `stream`; returns an mra_status value. */
 enum { MRA_LAYER_NORM = 0, MRA_RMS_NORM = 1 };

@@ -320,9 +320,11 @@ def _call_on(index, stream, workspace_bytes, call):
         return _call_on(index, None, workspace_bytes, call)
 
 
+# Sizes of workspaces go by the SMs of the device that is current (kept per device).
 @functools.lru_cache(maxsize=256)
-def _bias_workspace(B, H, N, D, cap, nb, dtype, backward):
-    return load_library().mra_blocksparse_attention_bias_workspace(B, H, N, D, cap, nb, dtype, backward)
+def _bias_workspace(index, B, H, N, D, cap, nb, dtype, backward):
+    with torch.cuda.device(index):
+        return load_library().mra_blocksparse_attention_bias_workspace(B, H, N, D, cap, nb, dtype, backward)
 
 
 def _bias_checks(where, q, k, v, key_mask, bias_table, bucket, lse, block_idx, scale, names, *like_q):
@@ -362,7 +364,7 @@ def mra_blocksparse_attention_bias_fwd(q, k, v, key_mask, bias_table, bucket, ou
     where = "mra_blocksparse_attention_bias_fwd"
     index, B, H, N, D, nb, cap, dtype, scale = _bias_checks(where, q, k, v, key_mask, bias_table, bucket, lse, block_idx,
                                                             scale, "q k v out", out)
-    size = _bias_workspace(B, H, N, D, cap, nb, dtype, 0)
+    size = _bias_workspace(index, B, H, N, D, cap, nb, dtype, 0)
     st = _call_on(index, stream, size, lambda ws, s: load_library().mra_blocksparse_attention_bias_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask), bias_table.data_ptr(), bucket.data_ptr(), nb, scale,
         out.data_ptr(), _addr(lse), B, H, N, D, _addr(block_idx), cap, dtype, ws, size, s))
@@ -382,7 +384,7 @@ def mra_blocksparse_attention_bias_bwd(q, k, v, key_mask, bias_table, bucket, ls
     index, B, H, N, D, nb, cap, dtype, scale = _bias_checks(where, q, k, v, key_mask, bias_table, bucket, lse, block_idx,
                                                             scale, "q k v dout dq dk dv", dout, dq, dk, dv)
     _expect_all(where, index, q.dtype, bias_table.shape, "dbias_table", dbias_table)
-    size = _bias_workspace(B, H, N, D, cap, nb, dtype, 1)
+    size = _bias_workspace(index, B, H, N, D, cap, nb, dtype, 1)
     st = _call_on(index, stream, size, lambda ws, s: load_library().mra_blocksparse_attention_bias_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask), bias_table.data_ptr(), bucket.data_ptr(), nb, scale,
         lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dbias_table.data_ptr(), B, H, N,
@@ -408,8 +410,9 @@ _NORMS = {"layer": MRA_LAYER_NORM, "rms": MRA_RMS_NORM}
 
 
 @functools.lru_cache(maxsize=256)
-def _norm_workspace(rows, hidden):
-    return load_library().mra_residual_norm_workspace(rows, hidden)
+def _norm_workspace(index, rows, hidden):
+    with torch.cuda.device(index):
+        return load_library().mra_residual_norm_workspace(rows, hidden)
 
 
 def _norm_checks(where, x, rows_names, rows_like, gate, names, weights, stats, norm, dgate=None):
@@ -466,7 +469,7 @@ def mra_residual_norm_bwd(x, h, stats, dx_out, dy, dx, dh, *, gate=None, post_no
         "post_w post_b pre_w pre_b dpost_w dpost_b dpre_w dpre_b",
         (post_w, post_b, pre_w, pre_b, dpost_w, dpost_b, dpre_w, dpre_b), stats, norm, dgate)
     norms = (MRA_NORM_POST if post_norm else 0) | (MRA_NORM_PRE if pre_norm else 0)
-    size = _norm_workspace(rows, hidden)
+    size = _norm_workspace(index, rows, hidden)
     st = _call_on(index, stream, size, lambda ws, s: load_library().mra_residual_norm_bwd(
         x.data_ptr(), _addr(h), _addr(gate), per, _addr(post_w), _addr(post_b), _addr(pre_w), _addr(pre_b), _addr(stats),
         _addr(dx_out), _addr(dy), _addr(dx), _addr(dh), _addr(dgate), _addr(dpost_w), _addr(dpost_b), _addr(dpre_w),
