@@ -283,7 +283,19 @@ def _expect_all(where, index, dtype, shape, names, *tensors):
             _expect(where, index, dtype, shape, **dict(zip(names.split(), tensors)))
 
 
-def _cuda_index(where, t):
+def _expect_each(where, index, dtype, shape, names, *tensors):
+    """_expect_all for tensors that must be given."""
+    for t in tensors:
+        if t is None:
+            missing = [n for n, x in zip(names.split(), tensors) if x is None]
+            raise ValueError(f"{where}: {missing[0]} must be given")
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            _expect(where, index, dtype, shape, **dict(zip(names.split(), tensors)))
+
+
+def _cuda_index(where, name, t):
+    if t is None:
+        raise ValueError(f"{where}: {name} must be given")
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{where}: tensors must be on a CUDA device")
@@ -328,18 +340,19 @@ def _bias_workspace(index, B, H, N, D, cap, nb, dtype, backward):
 
 
 def _bias_checks(where, q, k, v, key_mask, bias_table, bucket, lse, block_idx, scale, names, *like_q):
-    shape, dtype, index = q.shape, q.dtype, _cuda_index(where, q)
+    index = _cuda_index(where, "q", q)
+    shape, dtype = q.shape, q.dtype
     if len(shape) != 4 or 0 in shape:
         raise ValueError(f"{where}: q, k, v must be [B, H, N, D], none of them 0")
     if dtype not in _DTYPES:
         raise ValueError(f"{where}: q must be bf16 or fp32")
     B, H, N, D = shape
-    if bias_table.dim() != 2:
+    if bias_table is None or bias_table.dim() != 2:
         raise ValueError(f"{where}: bias_table must be [num_buckets, H]")
     nb, cap = bias_table.shape[0], 0
-    _expect_all(where, index, dtype, shape, names, q, k, v, *like_q)
-    _expect_all(where, index, dtype, (nb, H), "bias_table", bias_table)
-    _expect_all(where, index, torch.int32, (2 * N - 1,), "bucket", bucket)
+    _expect_each(where, index, dtype, shape, names, q, k, v, *like_q)
+    _expect_each(where, index, dtype, (nb, H), "bias_table", bias_table)
+    _expect_each(where, index, torch.int32, (2 * N - 1,), "bucket", bucket)
     if key_mask is not None:
         _expect_all(where, index, torch.float32, (B, N), "key_mask", key_mask)
     if lse is not None:
@@ -383,7 +396,7 @@ def mra_blocksparse_attention_bias_bwd(q, k, v, key_mask, bias_table, bucket, ls
         raise ValueError(f"{where}: lse of the forward pass is needed")
     index, B, H, N, D, nb, cap, dtype, scale = _bias_checks(where, q, k, v, key_mask, bias_table, bucket, lse, block_idx,
                                                             scale, "q k v dout dq dk dv", dout, dq, dk, dv)
-    _expect_all(where, index, q.dtype, bias_table.shape, "dbias_table", dbias_table)
+    _expect_each(where, index, q.dtype, bias_table.shape, "dbias_table", dbias_table)
     size = _bias_workspace(index, B, H, N, D, cap, nb, dtype, 1)
     st = _call_on(index, stream, size, lambda ws, s: load_library().mra_blocksparse_attention_bias_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask), bias_table.data_ptr(), bucket.data_ptr(), nb, scale,
@@ -406,9 +419,6 @@ def mra_relative_buckets(N: int, num_buckets: int, max_distance: int, bidirectio
     return out
 
 
-_NORMS = {"layer": MRA_LAYER_NORM, "rms": MRA_RMS_NORM}
-
-
 @functools.lru_cache(maxsize=256)
 def _norm_workspace(index, rows, hidden):
     with torch.cuda.device(index):
@@ -416,7 +426,8 @@ def _norm_workspace(index, rows, hidden):
 
 
 def _norm_checks(where, x, rows_names, rows_like, gate, names, weights, stats, norm, dgate=None):
-    shape, dtype, index = x.shape, x.dtype, _cuda_index(where, x)
+    index = _cuda_index(where, "x", x)
+    shape, dtype = x.shape, x.dtype
     if dtype not in _DTYPES or len(shape) < 1 or shape[-1] == 0:
         raise ValueError(f"{where}: x must be bf16 or fp32 [..., hidden]")
     if norm not in _NORMS:
