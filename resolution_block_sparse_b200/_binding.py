@@ -437,10 +437,10 @@ def _norm_checks(where, x, rows_names, rows_like, gate, names, weights, stats, n
     _expect_all(where, index, dtype, shape, rows_names, x, *rows_like)
     _expect_all(where, index, dtype, (hidden,), names, *weights)
     if gate is not None:
-        gates = gate.shape[0] if gate.dim() == 2 else 0
-        if gates < 1 or rows < 1 or rows % gates:
+        gates = gate.shape[0] if gate.dim() == 2 else -1
+        if gates < 0 or (rows and (gates == 0 or rows % gates)):
             raise ValueError(f"{where}: gate must be [rows, hidden] with a number of rows that divides x's")
-        per = max(1, rows // gates)
+        per = max(1, rows // max(1, gates))
         _expect_all(where, index, dtype, (gates, hidden), "gate dgate", gate, dgate)
     elif dgate is not None:
         raise ValueError(f"{where}: dgate without a gate")
@@ -487,6 +487,8 @@ def mra_residual_norm_bwd(x, h, stats, dx_out, dy, dx, dh, *, gate=None, post_no
         _addr(dpre_b), rows, hidden, kind, norms, residual_scale, eps, dtype, ws, size, s))
     if st != MRA_OK:
         raise MraError(st, where)
+    if rows == 0 and dgate is not None:
+        _call_on(index, stream, 0, lambda ws, s: dgate.zero_())     # an empty sum
     return dx, dh
 
 
