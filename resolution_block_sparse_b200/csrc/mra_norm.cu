@@ -52,8 +52,11 @@ constexpr int kSmemStep = 4096, kSmemSteps = 33;
 constexpr int kBackwardThreads = 512;
 // Threads of the backward kernel that one SM holds, by the registers they need:
 // eight columns in 16-byte pieces of bf16 and four single ones fit 128, and two
-// blocks of 320 with less beat one (2331 x 1027 fp32, step: 42 to 38.6 us; more
-// blocks of 256 with less do not, 8000 x 1001 bf16: 81 to 88 us).
+// blocks of 320 with less beat one of 512 at every width that 320 threads have
+// (1025 to 1280 single columns; 16000 rows, step, one / two: fp32 of 1025 239 / 201
+// us, 1153 247 / 210, 1275 251 / 215, bf16 of 1025 224 / 207, 1275 235 / 219; 300
+// rows: no difference).  More blocks of 256 with less do not (8000 x 1001 bf16:
+// 81 to 88 us).
 constexpr __host__ __device__ int resident_threads(int V, int threads) {
     return V == 1 && threads > 256 && threads <= 320 ? 640 : V != 4 ? kBackwardThreads : kBackwardThreads / 2;
 }
@@ -378,7 +381,9 @@ cudaError_t forward(const Args &a, cudaStream_t s) {
 }
 // A warp holds a row of up to 512 (32 lanes x 16) or, in 16-byte loads of
 // bf16, 1024 columns; longer rows take a block.  Registers decide how many
-// rows are on their way, so there is a variant for each quarter.
+// rows are on their way, so there is a variant for each quarter, and one of
+// five columns a thread for single columns up to 1280 (16000 rows, eight / five:
+// fp32 of 1025 117 / 79 us, 1275 119 / 84; bf16 of 1025 96 / 79, 1275 99 / 84).
 template <typename T>
 cudaError_t launch_forward(const Args &a, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
