@@ -80,7 +80,8 @@ typedef enum {
     MRA_ERR_DEVICE_TIMEOUT = 5,  /* a bounded device wait gave up (the MRA_DEV_TIMEOUT
                                     bit of a status word, see mra_status_from_device) */
     MRA_ERR_TOO_LARGE = 6        /* the problem needs more scratch than the static
-                                    array of mra_attention_fwd_noalloc holds         */
+                                    array of mra_attention_fwd_noalloc, or more room
+                                    than the caller's workspace or list, holds       */
 } mra_status;
 
 enum { MRA_FULL = 0, MRA_SPARSE = 1 };

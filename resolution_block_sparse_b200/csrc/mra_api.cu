@@ -758,7 +758,7 @@ const char *mra_status_string(int status) {
         case MRA_ERR_ALLOC: return "workspace allocation failed";
         case MRA_ERR_DEVICE_TIMEOUT: return "bounded device wait gave up";
         case MRA_ERR_TOO_LARGE:
-            return "problem needs more scratch than the no-allocation entry point's static array";
+            return "not enough scratch memory (the caller's workspace or list, or the no-allocation entry point's static array)";
         default: return "unknown status";
     }
 }

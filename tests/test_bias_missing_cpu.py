@@ -33,3 +33,7 @@ def test_norms():
         mra.mra_residual_norm_fwd(None, x, x, x)
     with pytest.raises(ValueError, match="mra_residual_norm_bwd: x "):
         mra.mra_residual_norm_bwd(None, x, x, x, x, x, x)
+
+
+def test_too_small_a_workspace_is_named():
+    assert "workspace" in mra.mra_status_string(6)
