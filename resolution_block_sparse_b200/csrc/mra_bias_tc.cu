@@ -19,8 +19,8 @@
 // that they may write): with weights of 0 in their place, a NaN or an infinity
 // in V, K, Q or dO would reach rows whose lists do not hold it.  So the
 // accumulators are zeros at an item's start, which its last reader sees to.
-// The two warps of a row share nothing in the loop: forward, each has a reference, a sum and an output accumulator of its own,
-// joined at the end.
+// The two warps of a row share nothing in the loop: forward, each has a
+// reference, a sum and an output accumulator of its own, joined at the end.
 //
 // Forward and delta have two buffers of scores in tensor memory: the next
 // step's products run during this step's softmax.  With its accumulators kRows
@@ -38,15 +38,16 @@
 // The MMA warp runs its role converged and an elected lane issues (lane 0
 // instead: 100 to 130 cycles to issue a product, train BigBird 370 us, not 343).
 //
-// What bounds it (clock stamps per role, N = 2048, all blocks, two blocks per
-// SM): the chains of the softmax warps, four a scheduler.  A step of 64 columns
-// takes them 2,740 cycles in kRows and 2,870 in kCols, 2,200 forward, against
-// 512 for its exponentials and 450 (forward) to 900 (kCols) in the tensor pipe,
-// where a product with N = 64 is bound by reading its operands (50 cycles from
-// shared memory, 65 with the weights in tensor memory, 32 of arithmetic).
-// Issue slots are 34 to 44 % used while blocks run; between two items the roles
-// leave about 4,000 cycles (a split group's partial result: 7,000), which the
-// SM's other block fills.
+// What bounds it (clock stamps per role, all blocks, two blocks per SM): the
+// chains of the softmax warps, four a scheduler.  A step of 64 columns takes them
+// 1,500 cycles forward (N = 4096), 2,740 in kRows and 2,870 in kCols (N = 2048).
+// Meanwhile the SM computes a step of each of its two blocks: 1,024 cycles of
+// exponentials and 900 (forward) to 1,800 (kCols) in the tensor pipe, where a
+// product with N = 64 is bound by reading its operands (50 cycles from shared
+// memory, 65 with the weights in tensor memory, 32 of arithmetic).  Issue slots
+// are 34 to 44 % used while blocks run; between two items the roles leave about
+// 4,000 cycles (a split group's partial result: 7,000), which the SM's other
+// block fills.
 //
 // Warps 0-7: softmax and epilogue; warp 8: items and TMA; warp 9: MMA issue.
 // Every wait is bounded: on expiry MRA_DEV_TIMEOUT is raised, every role stops,
