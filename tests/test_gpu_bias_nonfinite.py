@@ -36,7 +36,11 @@ WARP = {"warp-lists-d32": dict(B=2, H=4, N=700, D=32, dtype=BF16, lists=rows(6, 
         "warp-padded-d32": dict(B=3, H=2, N=150, D=32, dtype=BF16, pad=[70, 0, 33]),
         "warp-backward": dict(B=2, H=2, N=400, D=64, dtype=BF16, lists=rows(3, (1,), (0, 5)), pad=[0, 150]),
         "warp-backward-causal": dict(B=1, H=2, N=300, D=64, dtype=BF16, causal=True, pad=[90])}
-CASES = {**TC, **FP32, **WARP}
+SPLIT = {"split-tc-causal": dict(B=3, H=4, N=1300, D=64, dtype=BF16, causal=True, pad=[0, 500, 1]),
+         "split-forward-causal": dict(B=1, H=2, N=1200, D=64, dtype=BF16, causal=True),
+         "split-f32-causal": dict(B=1, H=2, N=1200, D=32, dtype=F32, causal=True),
+         "tc-short-causal": dict(B=8, H=8, N=600, D=64, dtype=BF16, causal=True, pad=[0, 90] + [0] * 6)}
+CASES = {**TC, **FP32, **WARP, **SPLIT}
 
 
 def make(name, seed=5):
